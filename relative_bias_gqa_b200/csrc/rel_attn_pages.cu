@@ -528,12 +528,13 @@ fork_kernel(const Book bk, const Work w, const int* src_rows, const int* dst_row
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, first = team.rank() * kThreads + threadIdx.x, step = team.ctas() * kThreads;
   if (first == 0) *w.copies = 0;
-  // a mark per row, against two forks into one
+  // a mark per row: of a destination 0 (against two forks into one), of another source -1
   __shared__ int near_marks[SOLO ? kSoloRows : 1];
   int* const marks = SOLO ? near_marks : w.name;
   for (int k = first; k < forks; k += step) {
-    const int d = __ldg(dst_rows + k);
+    const int d = __ldg(dst_rows + k), s = __ldg(src_rows + k);
     if ((unsigned)d < (unsigned)bk.rows) marks[d] = -1;
+    if ((unsigned)s < (unsigned)bk.rows) marks[s] = -1;
   }
   team.sync();
   unsigned bad = 0;
@@ -649,7 +650,12 @@ fork_kernel(const Book bk, const Work w, const int* src_rows, const int* dst_row
   });
   team.sync();                               // (every block has read the lengths)
   if (!team.ok) return;
-  for (int k = first; k < forks; k += step) bk.lens[__ldg(dst_rows + k)] = load(bk.lens + __ldg(src_rows + k));
+  // (a source that is a destination as well was free: its length, which another
+  // thread may have written by now, is not read)
+  for (int k = first; k < forks; k += step) {
+    const int s = __ldg(src_rows + k), mark = SOLO ? near_marks[s] : load(w.name + s);
+    bk.lens[__ldg(dst_rows + k)] = mark == -1 ? load(bk.lens + s) : 0;
+  }
   if (first == 0) *w.copies = (int)need;
 }
 

@@ -468,3 +468,31 @@ def test_captured_steps(gpu):
             table, refs, (pool,), count = oracle.pages_compact_ref(table, lens, refs, [pool])
             assert pages.read_status() == gpu.REL_ATTN_OK and int(live) == count
             same(r, refs), same(n, lens), same(t, table, lens), same(p, pool)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,forks", [(100, 40), (250, 120), (300, 140), (2100, 1000)])
+@pytest.mark.parametrize("backwards", [False, True])
+def test_free_rows_as_sources_that_the_same_call_fills(gpu, rows, forks, backwards):
+    """A chain in one call: its first forks fill rows that its last forks (of other
+    warps and blocks) have as sources, or the other way round; those sources count
+    as they were, free.  Ten times over, each from the same state."""
+    rng = np.random.default_rng(forks)
+    table, lens, refs = draw_book(rng, rows, 200, 3 * rows + forks * 4, free_rows=0.0)
+    lens[rows // 2:] = 0
+    refs = references(table, lens, len(refs)).astype(np.int32)
+    half = forks // 2
+    free = rows // 2 + rng.permutation(rows - rows // 2)
+    filled, chained = free[:half], free[half:forks]
+    src = np.concatenate([rng.choice(np.flatnonzero(lens > 0), half), filled]).astype(np.int32)
+    dst = np.concatenate([filled, chained]).astype(np.int32)
+    if backwards:
+        src, dst = src[::-1], dst[::-1]
+    want = oracle.pages_fork_ref(table, lens, refs, src, dst, False)
+    assert (want[1][chained] == 0).all() and (want[1][filled] > 0).all()
+    for _ in range(10):
+        t, n, r = to_gpu(table, lens, refs)
+        pages = gpu.Pages(t, n, r)
+        pages.fork(*to_gpu(src, dst))
+        assert pages.read_status() == gpu.REL_ATTN_OK
+        same(n, want[1]), same(r, want[2]), same(t, want[0], want[1])
