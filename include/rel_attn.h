@@ -419,10 +419,12 @@ size_t rel_attn_sink_prefill_workspace_bytes(const rel_attn_shape* shape, int wi
  * error, nothing; the workspace's status word (rel_attn_read_status) then
  * says REL_ATTN_ERR_NO_PAGES (too few free pages) or REL_ATTN_ERR_BAD_SEQ (a
  * length or row out of range, an entry outside the pool, an entry whose page
- * has no references).  (rel_attn_pages_compact passes over such rows and
- * entries, and reports them.)  After REL_ATTN_ERR_TIMEOUT (a wait of the
- * plan's blocks for one another ran out) the state may be partly changed, and
- * the workspace is initialised anew before its next use.
+ * has no references).  (rel_attn_pages_compact leaves such rows and entries as
+ * they are, compacts the rest and reports them: an entry whose page had no
+ * references may then name a page that another row's moved to.)  After
+ * REL_ATTN_ERR_TIMEOUT (a wait of the plan's blocks for one another ran out)
+ * the state may be partly changed, and the workspace is initialised anew
+ * before its next use.
  *   workspace  rel_attn_pages_workspace_bytes bytes, 256-byte aligned,
  *              initialised with rel_attn_workspace_init; one call at a time.
  */

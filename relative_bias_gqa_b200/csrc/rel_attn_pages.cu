@@ -678,16 +678,16 @@ __global__ void __launch_bounds__(Team<SOLO>::kThreads) compact_kernel(const Boo
   const int before = before_warp(team, c, &n, counts);
   if (!team.ok) return;
   // w.src takes the live pages at n and behind by rank from the end (they are
-  // as many as the holes, but how many is not known yet), w.dst the holes; the
-  // free pages at n and behind keep their name
+  // as many as the holes, but how many is not known yet), w.dst the holes; a
+  // live page keeps its name until it moves, a free one has none
   for_matching(bk.refs, s, is_live, [&](int page, bool in, bool hit, int rank) {
     rank += before;
     if (in && page >= n) {
       if (hit) w.src[n - 1 - rank] = page;
-      w.name[page] = page;
     } else if (in && !hit) {
       w.dst[page - rank] = page;
     }
+    if (in) w.name[page] = hit ? page : -1;
     if (in && page == n) *w.copies = n - rank;   // holes = live pages at n and behind
   });
   if (first == 0) {
@@ -720,7 +720,7 @@ struct Pools {
 // Copies w.copies pages (w.src to w.dst, no page on both sides) in every
 // pool (16 KB to a block at a time, 64 bytes in flight to a thread: 1.11 GB read
 // and written in 179 us, 6.2 TB/s); with `rename`, also gives the block table's
-// entries their new names.
+// entries their new names, and reports those that name no live page.
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(const __grid_constant__ Pools<N> pools, const Book bk, const Work w, const int* num_live, int rename) {
@@ -728,21 +728,26 @@ copy_kernel(const __grid_constant__ Pools<N> pools, const Book bk, const Work w,
   ptx::pdl_wait_primary();
   if (*w.status & kStatusBitTimeout) return;      // (the plan is not whole)
   const int copies = *w.copies;
-  if (rename && copies > 0) {
+  if (rename) {
+    // (where no page moves too: every entry is looked at, whether it names a live page)
     const int n = *num_live;
+    bool bad = false;
     for (int b = blockIdx.x; b < bk.rows; b += gridDim.x) {
       const int L = bk.lens[b];
       if ((unsigned)L > (unsigned)bk.width * kKeys) {
-        if (threadIdx.x == 0) atomicOr(w.status, kStatusBitBadSeq);
+        bad = true;
         continue;
       }
       for (int i = threadIdx.x; i < ceil_pages(L); i += kCopyThreads) {
         int* e = bk.table + (size_t)b * bk.width + i;
         const int page = *e;
-        if (page >= bk.num_pages) atomicOr(w.status, kStatusBitBadSeq);
-        else if (page >= n) *e = w.name[page];
+        if (page < 0) continue;
+        const int name = page < bk.num_pages ? w.name[page] : -1;
+        if (name < 0) bad = true;
+        else if (page >= n) *e = name;
       }
     }
+    if (bad) atomicOr(w.status, kStatusBitBadSeq);
   }
   const unsigned long long units = (unsigned long long)copies * pools.chunks;
   for (unsigned long long u = blockIdx.x; u < units; u += gridDim.x) {

@@ -496,3 +496,39 @@ def test_free_rows_as_sources_that_the_same_call_fills(gpu, rows, forks, backwar
         pages.fork(*to_gpu(src, dst))
         assert pages.read_status() == gpu.REL_ATTN_OK
         same(n, want[1]), same(r, want[2]), same(t, want[0], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,longest,spare", [(12, 900, 60), (300, 600, 300), (20, 300, 40_000)])
+@pytest.mark.parametrize("moves", [False, True])
+def test_compact_reports_a_bad_book(gpu, rows, longest, spare, moves):
+    """A length out of range, an entry outside the pool and one whose page has no
+    references, each by itself, where pages move and where none does: left as they
+    were, reported, and the rest compacted as if they were not there."""
+    rng = np.random.default_rng(rows)
+    table, lens, refs = draw_book(rng, rows, longest, spare, free_rows=0.1)
+    lens[:3] = longest // 2
+    table[:3, :-(-longest // 128)] = -1
+    refs = references(table, lens, len(refs)).astype(np.int32)
+    if not moves:
+        table, refs, _, _ = oracle.pages_compact_ref(table, lens, refs)
+        refs = refs.astype(np.int32)
+    hole = np.flatnonzero(refs == 0)
+    faults = [dict(length=-1), dict(length=table.shape[1] * 64 + 1), dict(entry=len(refs)), dict(entry=2 ** 31 - 1),
+              dict(entry=int(hole[0])), dict(entry=int(hole[-1]))]
+    for fault in faults:
+        bad, long = table.astype(np.int32), lens.copy()
+        if "length" in fault:
+            long[1] = fault["length"]
+        else:
+            bad[1, 2] = fault["entry"]
+        t, n, r = to_gpu(bad, long, refs)
+        pages, live = gpu.Pages(t, n, r), torch.zeros(1, dtype=torch.int32, device="cuda")
+        pages.compact(live)
+        assert pages.read_status() == gpu.REL_ATTN_ERR_BAD_SEQ and pages.read_status() == gpu.REL_ATTN_OK
+        want, want_refs, _, count = oracle.pages_compact_ref(table, lens, refs)
+        assert (want_refs != refs).any() == moves
+        if "entry" in fault:
+            want[1, 2] = fault["entry"]
+        assert int(live) == count
+        same(r, want_refs), same(n, long), same(t, want, lens)
