@@ -208,23 +208,22 @@ void fill_max_spans(EdgeEntry& e) {
   }
 }
 
+// The table's entry, made if it is not there; g_cache_mu is held, and the
+// entry is its own only as long as that.
+const EdgeEntry& edge_entry(const rel_attn_shape* s) {
+  for (auto& e : g_edge_cache)
+    if (e.nb == s->num_buckets && e.e == s->exact_buckets && e.dmax == s->max_distance) return e;
+  EdgeEntry& e = g_edge_cache[g_edge_next++ % kEdgeCache];
+  bucket_table(s, &e.ex, &e.nl, e.edges, &e.log2_ex, &e.log_scale);
+  e.nb = s->num_buckets; e.e = s->exact_buckets; e.dmax = s->max_distance;
+  fill_max_spans(e);
+  return e;
+}
+
 void bucket_table_cached(const rel_attn_shape* s, int* ex, int* nl, int* edges,
                          float* log2_ex = nullptr, float* log_scale = nullptr) {
   std::lock_guard<std::mutex> lk(g_cache_mu);
-  const EdgeEntry* hit = nullptr;
-  for (auto& e : g_edge_cache) {
-    if (e.nb == s->num_buckets && e.e == s->exact_buckets && e.dmax == s->max_distance) {
-      hit = &e;
-      break;
-    }
-  }
-  if (!hit) {
-    EdgeEntry& e = g_edge_cache[g_edge_next++ % kEdgeCache];
-    bucket_table(s, &e.ex, &e.nl, e.edges, &e.log2_ex, &e.log_scale);
-    e.nb = s->num_buckets; e.e = s->exact_buckets; e.dmax = s->max_distance;
-    fill_max_spans(e);
-    hit = &e;
-  }
+  const EdgeEntry* hit = &edge_entry(s);
   *ex = hit->ex;
   *nl = hit->nl;
   if (log2_ex) *log2_ex = hit->log2_ex;
@@ -239,14 +238,9 @@ void bucket_table_cached(const rel_attn_shape* s, int* ex, int* nl, int* edges,
 // range can span more; such tables are rejected.  kernel_tokens is the T the
 // partial kernel runs with (1 for the E4M3 kernel, whose tokens are chunks).
 int cached_span(const rel_attn_shape* s, int kernel_tokens, bool page) {
-  int ex, nl;
-  static thread_local int edges[kMaxTailBuckets + 1];
-  bucket_table_cached(s, &ex, &nl, edges);
   std::lock_guard<std::mutex> lk(g_cache_mu);
-  for (auto& e : g_edge_cache)
-    if (e.nb == s->num_buckets && e.e == s->exact_buckets && e.dmax == s->max_distance)
-      return page ? e.page_span[kernel_tokens] : e.max_span[kernel_tokens];
-  return 0;
+  const EdgeEntry& e = edge_entry(s);
+  return page ? e.page_span[kernel_tokens] : e.max_span[kernel_tokens];
 }
 bool bucket_span_fits(const rel_attn_shape* s, int kernel_tokens) {
   const int span = cached_span(s, kernel_tokens, false);

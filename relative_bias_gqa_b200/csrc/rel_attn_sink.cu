@@ -97,8 +97,8 @@ bool tiled(const rel_attn_shape* s, bool e4m3, bool prefill) {
   return host::page_bucket_span(s, s->q_tokens) > (s->q_tokens == 1 ? 64 : 72);
 }
 
-int choose_splits(const rel_attn_shape* s, int window, int sinks, int sm_count, bool e4m3, bool prefill) {
-  return tiled(s, e4m3, prefill) ? splits_tiles(s, window, sinks, sm_count) : splits_steps(s, window, sinks, sm_count);
+int choose_splits(const rel_attn_shape* s, int window, int sinks, int sm_count, bool tiles) {
+  return tiles ? splits_tiles(s, window, sinks, sm_count) : splits_steps(s, window, sinks, sm_count);
 }
 
 bool off(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0; }
@@ -163,7 +163,7 @@ int run(const rel_attn_shape* s, const void* q, const void* k_cache, const void*
   rc = host::current_device(&dev, &sms);
   if (rc != REL_ATTN_OK) return rc;
   const bool tiles = tiled(s, e4m3, prefill);
-  int splits = num_splits > 0 ? num_splits : choose_splits(s, window, sinks, sms, e4m3, prefill);
+  int splits = num_splits > 0 ? num_splits : choose_splits(s, window, sinks, sms, tiles);
   const bool merged = splits == 1 || (!tiles && splits <= kMaxCluster);        // in the same launch
   if (!merged && bytes < host::workspace_bytes(s, splits)) {
     if (!prefill) return REL_ATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -206,12 +206,13 @@ int run(const rel_attn_shape* s, const void* q, const void* k_cache, const void*
 
 size_t workspace_bytes(const rel_attn_shape* s, int window, int sinks, int splits, bool e4m3, bool prefill) {
   if (check_shape(s, window, sinks, prefill) != REL_ATTN_OK || splits > 256) return 0;
+  const bool tiles = tiled(s, e4m3, prefill);
   if (splits <= 0) {
     int dev, sms;
     if (host::current_device(&dev, &sms) != REL_ATTN_OK) sms = 148;
-    splits = choose_splits(s, window, sinks, sms, e4m3, prefill);
+    splits = choose_splits(s, window, sinks, sms, tiles);
   }
-  return splits == 1 || (!tiled(s, e4m3, prefill) && splits <= kMaxCluster) ? kWorkspaceHeader : host::workspace_bytes(s, splits);
+  return splits == 1 || (!tiles && splits <= kMaxCluster) ? kWorkspaceHeader : host::workspace_bytes(s, splits);
 }
 
 }  // namespace

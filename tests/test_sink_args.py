@@ -4,6 +4,9 @@ the oracle pinned to the windowed decode's and to sums written out."""
 
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -131,3 +134,38 @@ def test_oracle_is_the_formula_written_out():
                  for j in sees]
             o = sum(x * c.v_cache[page, 0, j].double().numpy() for x, j in zip(w, sees)) / sum(w)
             assert np.abs(out[0, t, h] - o).max() < 1e-12 and abs(lse[0, t, h] - math.log(sum(w))) < 1e-12
+
+
+THREADS = r"""
+#include <atomic>
+#include <chrono>
+#include <thread>
+#include <vector>
+#include "rel_attn.h"
+// 32 threads, a dense bucket table each: its steps go to the tiles, whose two
+// splits need room, whatever tables the other threads ask for meanwhile.
+int main() {
+  std::vector<std::thread> threads;
+  std::atomic<int> wrong{0};
+  const auto end = std::chrono::steady_clock::now() + std::chrono::seconds(5);
+  for (int i = 0; i < 32; ++i)
+    threads.emplace_back([&, i] {
+      const rel_attn_shape dense = {2, 1, 12, 2, 128, 64, 50, 1000, 90 + i, 1, 60, 0, 0};
+      while (std::chrono::steady_clock::now() < end)
+        wrong += rel_attn_sink_workspace_bytes(&dense, 500, 4, 2) <= 256;
+    });
+  for (auto& t : threads) t.join();
+  return wrong != 0;
+}
+"""
+
+
+def test_bucket_spans_while_other_threads_use_other_tables(ra, tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("needs g++")
+    (tmp_path / "threads.cc").write_text(THREADS)
+    exe, where = tmp_path / "threads", os.path.dirname(build_mod.LIB_PATH)
+    subprocess.run([cxx, "-O2", "-std=c++17", "-I", build_mod.INCLUDE, str(tmp_path / "threads.cc"), "-o", str(exe), "-L", where,
+                    "-lrel_attn", f"-Wl,-rpath,{where}", "-lpthread"], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
