@@ -156,7 +156,9 @@ def make_shape(*, batch, q_tokens, num_q_heads, num_kv_heads, num_pages,
 def shape_of(q, k_cache, block_table, rel_table, *, max_seq_len=0, out_fp32=False,
              exact_buckets=1024, max_distance=1 << 20) -> RelAttnShape:
     B, T, Hq, D = q.shape
-    num_pages, Hkv, P, _ = k_cache.shape
+    num_pages, Hkv, P, dim = k_cache.shape
+    if dim != D or rel_table.shape[-1] != D:
+        raise ValueError(f"head dims differ: q {D}, k_cache {dim}, rel_table {rel_table.shape[-1]}")
     return make_shape(batch=B, q_tokens=T, num_q_heads=Hq, num_kv_heads=Hkv,
                       num_pages=num_pages, max_pages_per_seq=block_table.shape[1],
                       num_buckets=rel_table.shape[1], head_dim=D, page_size=P,

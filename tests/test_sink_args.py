@@ -93,6 +93,18 @@ def test_tensors_are_checked(ra):
         ra.rel_attn_sink_prefill(q[0], kv, kv, table, lens, rel, 5)
 
 
+def test_head_dims_that_differ_are_refused(ra):
+    """A cache of another head dim than the queries' would be read past its end:
+    refused where every call makes its shape."""
+    q = torch.zeros(1, 1, 6, 128, dtype=torch.bfloat16)
+    table, kv, rel = (torch.zeros(*s) for s in ((1, 2), (3, 1, 64, 128), (1, 8, 128)))
+    assert ra.shape_of(q, kv, table, rel).head_dim == 128
+    with pytest.raises(ValueError, match="head dims"):
+        ra.shape_of(q, kv[..., :64], table, rel)
+    with pytest.raises(ValueError, match="head dims"):
+        ra.shape_of(q, kv, table, rel[..., :64])
+
+
 # ------------------------------------------------------------------ oracle
 def case(lens, T, **kw):
     return W.make_case(seq_lens=lens, q_tokens=T, num_q_heads=4, num_kv_heads=1, rel_std=0.5, **kw)
