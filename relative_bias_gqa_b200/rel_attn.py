@@ -474,6 +474,12 @@ def _check_rows(name, t, like) -> None:
         raise ValueError(f"{name} must be a contiguous torch.int32 tensor of one dimension on {like.device}")
 
 
+def _check_written(name, t, device, host=False) -> None:
+    """Memory that kernels on ``device`` write: its own, or (``host``) mapped pinned host memory."""
+    if t.device != device and not (host and t.device.type == "cpu" and t.is_pinned()):
+        raise ValueError(f"{name} is on {t.device}, not on {device}" + (" or in pinned host memory" if host else ""))
+
+
 def _codes(t):
     return t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
 
@@ -526,8 +532,12 @@ class SinkPrepared:
         # (out and lse may also be mapped pinned host memory)
         for name, t, dt, shape in (("out", out, torch.float32 if out_fp32 else torch.bfloat16, q.shape),
                                    ("lse", lse, torch.float32, q.shape[:3])):
-            if t is not None and (t.dtype != dt or not t.is_contiguous() or tuple(t.shape) != tuple(shape)):
-                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)}")
+            if t is not None:
+                if t.dtype != dt or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+                    raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)}")
+                _check_written(name, t, q.device, host=True)
+        if workspace is not None:
+            _check_written("workspace", workspace.buf, q.device)
         self.shape = shape_of(q, k_cache, block_table, rel_table, max_seq_len=max_seq_len, out_fp32=out_fp32,
                               exact_buckets=exact_buckets, max_distance=max_distance)
         if workspace is None:
@@ -627,6 +637,7 @@ class Pages:
                 raise RelAttnError(REL_ATTN_ERR_INVALID_ARG)
             with _on(stream):
                 workspace = Workspace(need, block_table.device)
+        _check_written("workspace", workspace.buf, block_table.device)
         self.workspace = workspace
         self._book, self._count = ctypes.byref(self._c), ctypes.c_int(len(pools))
         self._ws = (ctypes.c_void_p(workspace.buf.data_ptr()), ctypes.c_size_t(workspace.nbytes))

@@ -105,6 +105,16 @@ def test_head_dims_that_differ_are_refused(ra):
         ra.shape_of(q, kv, table, rel[..., :64])
 
 
+def test_memory_that_kernels_cannot_write_is_refused(ra):
+    from relative_bias_gqa_b200.rel_attn import _check_written
+    cuda, here = torch.device("cuda", 0), torch.zeros(4)
+    for host in (False, True):
+        with pytest.raises(ValueError, match="out is on cpu"):
+            _check_written("out", here, cuda, host=host)
+        with pytest.raises(ValueError, match="out is on meta"):
+            _check_written("out", here.to("meta"), cuda, host=host)
+
+
 # ------------------------------------------------------------------ oracle
 def case(lens, T, **kw):
     return W.make_case(seq_lens=lens, q_tokens=T, num_q_heads=4, num_kv_heads=1, rel_std=0.5, **kw)
