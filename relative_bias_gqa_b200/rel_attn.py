@@ -619,6 +619,8 @@ class Pages:
         if block_table.dim() != 2:
             raise ValueError("block_table has 2 dimensions")
         rows, n = block_table.shape[0], page_refs.numel()
+        if n == 0:
+            raise ValueError("page_refs is empty: a pool has at least one page")
         _check_tensors([("block_table", block_table, torch.int32, None), ("seq_lens", seq_lens, torch.int32, (rows,)),
                         ("page_refs", page_refs, torch.int32, (n,))])
         pools = tuple(pools)

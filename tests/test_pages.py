@@ -132,6 +132,13 @@ def test_cpu_tensors_are_refused(ra):
         ra.Pages(z(2, 3), z(2), z(9))
 
 
+def test_an_empty_pool_is_refused(ra):
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    for pools in ((), (z(0, 16),)):
+        with pytest.raises(ValueError, match="at least one page"):
+            ra.Pages(z(2, 3), z(2), z(0), pools)
+
+
 # --------------------------------------------------------------------- GPU
 RESIZE = [dict(rows=1, longest=1, spare=3), dict(rows=1, longest=5000, spare=200), dict(rows=7, longest=300, spare=40),
           dict(rows=33, longest=2000, spare=500, window=100, sinks=70), dict(rows=300, longest=900, spare=3000, window=1, sinks=0),
