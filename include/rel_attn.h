@@ -429,9 +429,9 @@ size_t rel_attn_sink_prefill_workspace_bytes(const rel_attn_shape* shape, int wi
  *              initialised with rel_attn_workspace_init; one call at a time.
  */
 typedef struct rel_attn_pages {
-  int num_seqs;          /* rows of the block table, >= 1                        */
-  int max_pages_per_seq; /* entries of a row; * 64 < 2^31                        */
-  int num_pages;         /* pages of every pool                                  */
+  int num_seqs;          /* rows of the block table, 1 .. 2^30                   */
+  int max_pages_per_seq; /* entries of a row, >= 1; * 64 < 2^31                  */
+  int num_pages;         /* pages of every pool, 1 .. 2^30                       */
   int32_t* block_table;
   int32_t* seq_lens;
   int32_t* page_refs;

@@ -777,10 +777,14 @@ namespace {
 
 bool off(const void* p, uintptr_t a) { return !p || (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+// (rows and pages up to 2^30: the loops over them step past the last by less than that)
+bool sizes_fit(const rel_attn_pages* p) {
+  return p && p->num_seqs >= 1 && p->num_seqs <= (1 << 30) && p->max_pages_per_seq >= 1 && p->num_pages >= 1 &&
+         p->num_pages <= (1 << 30) && (long long)p->max_pages_per_seq * kKeys < (1ll << 31);
+}
+
 int check(const rel_attn_pages* p, const void* workspace, size_t bytes) {
-  if (!p || p->num_seqs < 1 || p->max_pages_per_seq < 1 || p->num_pages < 1 ||
-      (long long)p->max_pages_per_seq * kKeys >= (1ll << 31))
-    return REL_ATTN_ERR_INVALID_ARG;
+  if (!sizes_fit(p)) return REL_ATTN_ERR_INVALID_ARG;
   if (off(p->block_table, 4) || off(p->seq_lens, 4) || off(p->page_refs, 4) || off(workspace, 256))
     return REL_ATTN_ERR_INVALID_ARG;
   return bytes < work_bytes(p->num_seqs, p->max_pages_per_seq, p->num_pages) ? REL_ATTN_ERR_WORKSPACE_TOO_SMALL : REL_ATTN_OK;
@@ -859,7 +863,7 @@ int copy_pages(const rel_attn_pool* pools, int count, const Book& bk, const Work
 using namespace relattn;
 
 extern "C" size_t rel_attn_pages_workspace_bytes(const rel_attn_pages* p) {
-  if (!p || p->num_seqs < 1 || p->max_pages_per_seq < 1 || p->num_pages < 1) return 0;
+  if (!pages::sizes_fit(p)) return 0;
   return pages::work_bytes(p->num_seqs, p->max_pages_per_seq, p->num_pages);
 }
 

@@ -132,6 +132,17 @@ def test_cpu_tensors_are_refused(ra):
         ra.Pages(z(2, 3), z(2), z(9))
 
 
+@pytest.mark.parametrize("kw", [dict(num_seqs=0), dict(max_pages_per_seq=1 << 25), dict(num_seqs=(1 << 30) + 1), dict(num_pages=(1 << 30) + 1),
+                                dict(num_pages=(1 << 31) - 1), dict(num_seqs=(1 << 31) - 1)])
+def test_sizes_out_of_range_are_refused(ra, kw):
+    """... by the calls and by the query of their workspace alike."""
+    b, ok, lib = ctypes.byref(book(ra, **kw)), 1 << 20, ra.lib
+    assert lib.rel_attn_pages_workspace_bytes(b) == 0
+    assert lib.rel_attn_pages_resize(b, ok, 0, 0, ok, 1 << 60, None) == ra.REL_ATTN_ERR_INVALID_ARG
+    assert lib.rel_attn_pages_fork(b, ok, ok, 1, 0, None, 0, ok, 1 << 60, None) == ra.REL_ATTN_ERR_INVALID_ARG
+    assert lib.rel_attn_pages_compact(b, None, 0, ok, ok, 1 << 60, None) == ra.REL_ATTN_ERR_INVALID_ARG
+
+
 def test_an_empty_pool_is_refused(ra):
     z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     for pools in ((), (z(0, 16),)):
