@@ -352,6 +352,8 @@ int rel_attn_kv_write(const rel_attn_shape* shape, const void* k_new, const void
  * sees reaches none.  bf16 outputs are formed with the softmax weights rounded
  * once to the matrix instructions' type (bf16, or f16), fp32 outputs with the
  * weights in three bf16 or two f16 parts.
+ * Values are summed before the division by the weights' sum: up to 2^80 in
+ * magnitude (over codes: v_scale up to 2^64) the sums stay finite.
  */
 int rel_attn_sink_decode(const rel_attn_shape* shape, const void* q,
                          const void* k_cache, const void* v_cache,

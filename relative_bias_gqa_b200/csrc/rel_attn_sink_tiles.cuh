@@ -32,7 +32,8 @@
 // The reference of a row's exponentials is the maximum of the first page that
 // it sees anything of (the tile's first or second page, as a tile is shorter
 // than a page) and stays: weights are bf16, whose exponents reach 2^127, and
-// sums are fp32, so that a later weight may be 2^64 of the first.  Nothing is
+// sums are fp32, so that a later weight may be far above the first page's: a
+// row's may sum to 2^40 (of which 2^80 are left for the values).  Nothing is
 // handed from page to page, no maximum is sought on the pages behind, and O is
 // never rescaled.  A row that did go further shows in its sum; its tile is gone
 // over again at the end of the round, once for the maxima, once with them as
@@ -52,7 +53,10 @@
 namespace relattn {
 namespace sink {
 
-constexpr float kReach = 18446744073709551616.f;    // 2^64: how far a weight may lie above its reference's
+// 2^40: what a row's weights may sum to (28 nats above the first page's maximum).
+// |O| <= sum * max|v|, so that values up to 2^80 leave it finite.  (At 2^64 those
+// above 2^63 could come out as infinities.)
+constexpr float kReach = 1099511627776.f;
 constexpr int kRound = 64;                          // tiles a block does between two looks at what went further
 
 template <int G, bool KV8, bool THREE>
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(512, 1) sink_tiles_kernel(const __grid_constan
                 m = first_at[0];
                 if (n > 1 && m == -INFINITY) m = first_at[128];
                 m_forced = max3(top[0], top[128], K::kGroups == 3 ? top[256] : -INFINITY);
-                // (a weight above 2^64 makes the sum so)
+                // (a weight above kReach makes the sum so)
                 if (!again && total > kReach && r < K::kTokens * G && tok < t.tokens) marks[j] = 1;
               }
               if (part >= 0) {
