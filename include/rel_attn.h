@@ -378,6 +378,11 @@ int rel_attn_sink_decode_e4m3(const rel_attn_shape* shape, const void* q,
  *               rel_attn_workspace_init.  Where the query tiles are few, the
  *               keys are split as well if it has the bytes of
  *               rel_attn_sink_prefill_workspace_bytes(shape, window, num_sinks).
+ * Of a value that is not finite, tokens 95 or more positions before it, and
+ * those behind whose window begins 95 or more positions after it, see nothing
+ * (the latter but for values in the pages of the sinks); nearer ones that do
+ * not see it may be reached.  A key that is not finite reaches the tokens that
+ * see it alone.
  */
 int rel_attn_sink_prefill(const rel_attn_shape* shape, const void* q,
                           const void* k_cache, const void* v_cache,
