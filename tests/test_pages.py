@@ -550,3 +550,42 @@ def test_compact_reports_a_bad_book(gpu, rows, longest, spare, moves):
             want[1, 2] = fault["entry"]
         assert int(live) == count
         same(r, want_refs), same(n, long), same(t, want, lens)
+
+
+@pytest.mark.gpu
+def test_captured_steps_of_a_large_plan(gpu):
+    """resize and fork in one graph, compact in another, replayed in turn: a plan of
+    a block per SM, and both graphs on one workspace."""
+    rng = np.random.default_rng(8)
+    rows = 300
+    table, lens, refs = draw_book(rng, rows, 900, 4000, width=40)
+    lens[-60:] = 0
+    refs = references(table, lens, len(refs)).astype(np.int32)
+    pool = rng.integers(0, 1 << 30, (len(refs), 4), dtype=np.int32)
+    t, n, r, p = to_gpu(table, lens, refs, pool)
+    new, src, dst = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (rows, 20, 20))
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pages = gpu.Pages(t, n, r, [p])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(one, stream=s):
+            pages.resize(new, 300, 10)
+            pages.fork(src, dst)
+        with torch.cuda.graph(two, stream=s):
+            pages.compact(live)
+        for step in range(6):
+            to = np.minimum(np.where(lens > 0, lens + rng.integers(-5, 80, rows), 0).clip(0), 1500).astype(np.int32)
+            to[-60:] = 0
+            a, b = rng.integers(0, rows - 60, 20).astype(np.int32), (rows - 60 + rng.permutation(60)[:20]).astype(np.int32)
+            for x, y in ((new, to), (src, a), (dst, b)):
+                x.copy_(torch.from_numpy(y))
+            one.replay()
+            two.replay()
+            s.synchronize()
+            table, lens, refs = oracle.pages_resize_ref(table, lens, refs, to, 300, 10)
+            table, lens, refs, (pool,) = oracle.pages_fork_ref(table, lens, refs, a, b, False, [pool])
+            table, refs, (pool,), count = oracle.pages_compact_ref(table, lens, refs, [pool])
+            assert pages.read_status() == gpu.REL_ATTN_OK and int(live) == count
+            same(r, refs), same(n, lens), same(t, table, lens), same(p, pool)
