@@ -31,7 +31,14 @@ namespace pages {
 
 constexpr int kKeys = 64;                 // positions of a page
 constexpr int kSoloThreads = 1024, kTeamThreads = 512;
-constexpr int kSoloPages = 32768, kSoloRows = 256;   // plans up to these sizes are one block's
+// Plans up to these sizes are one block's.  One block / a block per SM, us: resize
+// of 16 rows 5.8 / 10.1, 64 rows 6.9 / 10.3, 256 rows 12.0 / 11.8 (lengths to 2,000);
+// 64 rows to 60,000 12.1 / 11.7, 512 rows to 2,000 20.6 / 12.4; fork of 8 rows to
+// 60,000 14.3 / 17.7, 32 to 2,000 11.7 / 17.3, 128 to 2,000 20.6 / 19.0; compact of
+// 2,311 pages 7.3 / 10.3, 9,728 15.1 / 15.0.  The rule goes by what a book may hold,
+// not by what a call changes: at both limits one block is the slower one (resize of
+// 256 rows to 16,000, 30,558 pages, 19.6 / 12.0; compact of 25,901 pages 31.9 / 26.5).
+constexpr int kSoloPages = 32768, kSoloRows = 256;
 constexpr int kMaxCtas = 256;
 constexpr unsigned long long kBroken = 1ull << 63;   // among the arrivals: a wait at the barrier ran out
 constexpr int kMaxPools = 512;
@@ -41,7 +48,8 @@ constexpr int kChunk = kCopyThreads * 16 * 4;   // bytes a copying CTA moves at 
 // tasks (its 32 warps go through them in turn: 16 branches of rows of up to 1,563
 // entries 18.2 us, with 64 to a task 20.7), 2 where a block per SM has its share
 // (a warp's scattered atomics are what the others wait for: a server of 512 rows
-// 17.3 us, with 128 to a task 18.6).
+// 17.3 us, with 128 to a task 18.6).  (These with a copy of the state before each
+// call: 1.4 us of the one, 4.3 of the other.)
 constexpr int kSoloBlock = 256, kTeamBlock = 64;
 constexpr int kTasks = 1024;              // tasks a block holds at a time
 
@@ -55,8 +63,8 @@ struct Book {
 // Workspace.  In the header, behind the status word: the team's barrier, its
 // errors, the number of page copies.  Behind it: the blocks' counts, the pages
 // to copy of each task of a fork and the rank of the first of them, the free
-// (or destination) pages, the pages to copy, the new name of each page (a fork:
-// a mark per row).
+// (or destination) pages, the pages to copy, the new name of each page, -1 of a
+// free one (a fork: a mark per row).
 struct Work {
   unsigned* status;
   unsigned long long* arrived;
@@ -393,7 +401,11 @@ struct Plan {
 
 // Bound by the latencies of its phases: 8 rows 5.8 us (rows, give back, count,
 // pick, write: each a trip to L2); 512 rows over 484K pages 12.9 us, of which the
-// barriers are three times 1.8.
+// barriers are three times 1.8.  With a window a call goes over all entries between
+// the sinks and the window's start, given back long ago or not, as the state does
+// not say from where on: rows of 128K positions, window 1,024, one position more to
+// each, 8 rows 9.7 us, 64 rows (one block, 126,000 entries) 36, 512 rows of up to
+// that length (a block per SM) 14.
 template <bool SOLO>
 __global__ void __launch_bounds__(Team<SOLO>::kThreads)
 resize_kernel(const Book bk, const Work w, const int* new_lens, int window, int sinks) {

@@ -66,8 +66,11 @@ int splits_steps(const rel_attn_shape* s, int window, int sinks, int sm_count) {
 
 // Splits of the tile kernel: the fewest page times of the busiest SM, a tile's
 // beginning and end counted as kTileCost pages and the combine kernel as
-// kCombineCost.  (Over codes, 8 tokens and 1,024 keys: 2 sequences with 64/8
-// heads whole 28 us, in 8 16 us; 16 with 32/8 heads whole 33, in 2 51.)
+// kCombineCost.  8 tokens, chosen against every other count of splits: over codes
+// and 1,024 keys 2 sequences with 64/8 heads in 8 15.0 us (whole 25.1, in 6 14.7),
+// 16 with 32/8 heads whole 30.0 (in 2 48.0); over bf16 one with 48/8 heads and
+// 32K keys in 18 39.5 (whole 464, in 16 41.4), 16 over 1,024 keys whole 22.6 (in 2
+// 41.2), 8 in 2 24.4 (whole 20.9: the rule's worst case).
 int splits_tiles(const rel_attn_shape* s, int window, int sinks, int sm_count) {
   constexpr double kTileCost = 6, kCombineCost = 4;
   const int G = s->num_q_heads / s->num_kv_heads, per = 128 / G;
@@ -87,9 +90,9 @@ int splits_tiles(const rel_attn_shape* s, int window, int sinks, int sm_count) {
 
 // Several tokens go to the tile kernel.  Over codes those of up to 16 rows to a
 // KV head have a kernel of their own: (64 query heads, 8 KV heads) 16 sequences
-// of 2 tokens over 1,024 keys 26 us, as tiles 30; (32, 8) 32 sequences of 4
-// tokens over 512 keys 29 against 41.  With more rows tiles win: (32, 8) 16
-// sequences of 8 tokens over 1,024 keys 33 against 61.
+// of 2 tokens over 1,024 keys 26.1 us, as tiles 27.6; (32, 8) 32 sequences of 4
+// tokens over 512 keys 27.2 against 36.3.  With more rows tiles win: (32, 8) 16
+// sequences of 8 tokens over 1,024 keys 30 against 61.
 // (A page of those two kernels holds 64 or 72 relative rows: a table whose
 // indices lie further apart goes to the tiles as well.)
 bool tiled(const rel_attn_shape* s, bool e4m3, bool prefill) {

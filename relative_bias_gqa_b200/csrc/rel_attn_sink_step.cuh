@@ -384,6 +384,10 @@ __device__ __forceinline__ int f16_exponent(float big) {
 // the long window; a warp number that the compiler does not know to be the
 // warp's, 21.7 and 93; PARTS as a branch in one kernel, 20.1 for the batch.
 //
+// Weights are rounded once (bf16 over a bf16 cache, f16 over codes) where the
+// output is bf16 and rounded as coarsely itself; all their parts cost one sequence
+// 7.2 us against 6.4, the batch over codes 21.6 against 19.6, the long window 90
+// against 85.
 // PARTS (fp32 outputs): weights in all their parts, and a page's products summed
 // by themselves before they are added (the matrix instructions cut off what their
 // accumulator cannot hold: the long window 1.7e-6 off, relative, against 4.8e-7).
@@ -614,7 +618,9 @@ __global__ void __launch_bounds__(StepConfig<F8>::kThreads, 2) sink_step_kernel(
 // a quarter of a page's keys each.  The relative product goes through a strip of
 // shared memory of the warp's own, where each token's row is shifted.  Bound by
 // the latency of that chain: 16 sequences of 2 tokens over 1,024 keys (64/8
-// heads) 25 us, 32 of 4 tokens over 512 keys (32/8) 28 us.  (More rows: tiles.)
+// heads) 26 us, 32 of 4 tokens over 512 keys (32/8) 27 us, each of 34 MB that a
+// plain copy would take 5.7 us for.  (More rows: tiles.)  Weights are one f16
+// part where the output is bf16: 2^-11 of them beside the output's own 2^-8.
 __global__ void __launch_bounds__(CodesConfig::kThreads, 2) sink_codes_kernel(const __grid_constant__ Params p) {
   using K = CodesConfig;
   extern __shared__ uint8_t smem_raw[];

@@ -25,7 +25,9 @@
 // many instructions as the exponentials.
 //
 // The softmax weights are written back to tensor memory (bf16; three parts where
-// the output is fp32) as the A operand of O += P . V.  [S | X] and P have two
+// the output is fp32) as the A operand of O += P . V.  (One part, 2^-8 of a
+// weight, where the output is rounded as coarsely itself: with three 8K tokens
+// take 663 us against 341, verify steps 36.5 against 22.8.)  [S | X] and P have two
 // buffers; pages go round three groups of 128 threads (one thread a row), as
 // [S | X] is free again when a group has read it to registers.
 //
