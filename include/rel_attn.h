@@ -371,9 +371,9 @@ int rel_attn_sink_decode_e4m3(const rel_attn_shape* shape, const void* q,
 
 /*
  * rel_attn_sink_prefill / rel_attn_sink_prefill_e4m3 -- the same attention for
- * many query tokens per sequence: a prompt, or a chunk of one.  Shape, tokens and positions as for
- * rel_attn_prefill (q_tokens = C, 1 .. 2^20); window, num_sinks, seq_lens and
- * the block table as for rel_attn_sink_decode.
+ * many query tokens per sequence: a prompt, or a chunk of one.  Shape, tokens
+ * and positions as for rel_attn_prefill (q_tokens = C, 1 .. 2^20); window,
+ * num_sinks, seq_lens and the block table as for rel_attn_sink_decode.
  *   workspace   at least 256 bytes, 256-byte aligned, initialised with
  *               rel_attn_workspace_init.  Where the query tiles are few, the
  *               keys are split as well if it has the bytes of

@@ -500,7 +500,10 @@ class SinkPrepared:
     rel_attn_sink_prefill; with k_scale and v_scale their E4M3 forms) with
     every argument checked and marshalled once, for repeated launches over the
     same buffers.  ``run()`` launches it on the current stream (or the one
-    given) and returns (out, lse).  Tensors must stay alive and unmoved."""
+    given) and returns (out, lse).  ``num_splits`` is a decode's: with
+    ``prefill`` it is not used (the library splits by the number of query
+    tiles, where the workspace has the room).  out and lse may be in pinned
+    host memory.  Tensors must stay alive and unmoved."""
 
     def __init__(self, q, k_cache, v_cache, block_table, seq_lens, rel_table, window, num_sinks=0,
                  num_splits=0, *, prefill=False, out=None, lse=None, workspace=None, max_seq_len=0,
