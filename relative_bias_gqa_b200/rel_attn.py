@@ -166,6 +166,13 @@ def shape_of(q, k_cache, block_table, rel_table, *, max_seq_len=0, out_fp32=Fals
                       max_seq_len=max_seq_len, out_fp32=out_fp32)
 
 
+def _check_caches(k_cache, *others) -> None:
+    """Caches that one table names: read and written with k_cache's extents."""
+    for t in others:
+        if t.shape != k_cache.shape:
+            raise ValueError(f"caches differ: {tuple(k_cache.shape)} and {tuple(t.shape)}")
+
+
 def rel_attn_workspace_bytes(shape: RelAttnShape, num_splits: int = 0) -> int:
     return int(lib.rel_attn_workspace_bytes(ctypes.byref(shape), num_splits))
 
@@ -246,6 +253,7 @@ def rel_attn_decode(q, k_cache, v_cache, block_table, seq_lens, rel_table,
                         ("block_table", block_table, torch.int32), ("seq_lens", seq_lens, torch.int32)):
         if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
+    _check_caches(k_cache, v_cache)
     shape = shape_of(q, k_cache, block_table, rel_table, max_seq_len=max_seq_len,
                      out_fp32=out_fp32, exact_buckets=exact_buckets,
                      max_distance=max_distance)
@@ -284,6 +292,7 @@ def rel_attn_decode_e4m3(q, k_codes, v_codes, k_scale, v_scale, block_table, seq
                         ("block_table", block_table, torch.int32), ("seq_lens", seq_lens, torch.int32)):
         if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
+    _check_caches(k_codes, v_codes)
     shape = shape_of(q, k_codes, block_table, rel_table, max_seq_len=max_seq_len,
                      out_fp32=out_fp32, exact_buckets=exact_buckets, max_distance=max_distance)
     if out is None:
@@ -316,6 +325,7 @@ def rel_attn_prefill(q, k_cache, v_cache, block_table, seq_lens, rel_table, wind
                         ("block_table", block_table, torch.int32), ("seq_lens", seq_lens, torch.int32)):
         if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
+    _check_caches(k_cache, v_cache)
     shape = shape_of(q, k_cache, block_table, rel_table, max_seq_len=max_seq_len,
                      out_fp32=out_fp32, exact_buckets=exact_buckets, max_distance=max_distance)
     if out is None:
@@ -373,6 +383,9 @@ def rel_attn_kv_write(k_new, v_new, conv_w, k_raw, v_raw, k_cache, v_cache, bloc
         if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
     B, T, Hkv, D = k_new.shape
+    if tuple(k_cache.shape[1::2]) != (Hkv, D) or v_new.shape != k_new.shape or tuple(conv_w.shape) != (2, Hkv, D, 4):
+        raise ValueError("heads and head dims of k_new, v_new, conv_w and the caches differ")
+    _check_caches(k_cache, v_cache, k_raw, v_raw)
     shape = make_shape(batch=B, q_tokens=T, num_q_heads=Hkv, num_kv_heads=Hkv,
                        num_pages=k_cache.shape[0], max_pages_per_seq=block_table.shape[1],
                        num_buckets=1, head_dim=D, page_size=k_cache.shape[2])
@@ -396,6 +409,7 @@ class Prepared:
                  num_splits=0, *, out=None, lse=None, max_seq_len=0, out_fp32=False,
                  exact_buckets=1024, max_distance=1 << 20, stream=None, k_scale=None,
                  v_scale=None):
+        _check_caches(k_cache, v_cache)
         self.shape = shape_of(q, k_cache, block_table, rel_table, max_seq_len=max_seq_len,
                               out_fp32=out_fp32, exact_buckets=exact_buckets,
                               max_distance=max_distance)
