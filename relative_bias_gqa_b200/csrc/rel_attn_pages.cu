@@ -399,8 +399,8 @@ struct Plan {
   long long need, tasks, given;              // new pages, all tasks, those that give back
 };
 
-// Bound by the latencies of its phases: 8 rows 5.8 us (rows, give back, count,
-// pick, write: each a trip to L2); 512 rows over 484K pages 12.9 us, of which the
+// Bound by the latencies of its phases: 8 rows 6 us (rows, give back, count,
+// pick, write: each a trip to L2); 512 rows over 484K pages 13 us, of which the
 // barriers are three times 1.8.  With a window a call goes over all entries between
 // the sinks and the window's start, given back long ago or not, as the state does
 // not say from where on: rows of 128K positions, window 1,024, one position more to
