@@ -589,3 +589,39 @@ def test_captured_steps_of_a_large_plan(gpu):
             table, refs, (pool,), count = oracle.pages_compact_ref(table, lens, refs, [pool])
             assert pages.read_status() == gpu.REL_ATTN_OK and int(live) == count
             same(r, refs), same(n, lens), same(t, table, lens), same(p, pool)
+
+
+@pytest.mark.gpu
+def test_two_large_plans_at_once(gpu):
+    """Books of their own on two streams: each a block per SM, at the same time."""
+    rng, runs = np.random.default_rng(6), []
+    for rows in (300, 400):
+        table, lens, refs = draw_book(rng, rows, 2000, 30_000)
+        more = np.where(lens > 0, lens + 130, 0).astype(np.int32)
+        want = oracle.pages_resize_ref(*oracle.pages_resize_ref(table, lens, refs, more, 0, 0), lens, 0, 0)
+        t, n, r, up, down = to_gpu(table, lens, refs, more, lens)
+        s = torch.cuda.Stream()
+        runs.append((gpu.Pages(t, n, r, stream=s), up, down, want))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for pages, up, down, _ in runs:
+            pages.resize(up)
+            pages.resize(down)
+    torch.cuda.synchronize()
+    for pages, _, _, want in runs:
+        assert pages.read_status() == gpu.REL_ATTN_OK
+        same(pages.page_refs, want[2]), same(pages.seq_lens, want[1]), same(pages.block_table, want[0], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (-2 ** 31, 5)])
+def test_resize_with_the_largest_windows_and_sinks(gpu, window, sinks):
+    rng = np.random.default_rng(3)
+    table, lens, refs = draw_book(rng, 20, 900, 200)
+    t, n, r = to_gpu(table, lens, refs)
+    pages = gpu.Pages(t, n, r)
+    new = np.maximum(0, lens + rng.integers(-70, 150, 20)).astype(np.int32)
+    table, lens, refs = oracle.pages_resize_ref(table, lens, refs, new, window, sinks)
+    pages.resize(*to_gpu(new), window, sinks)
+    assert pages.read_status() == gpu.REL_ATTN_OK
+    same(r, refs), same(n, lens), same(t, table, lens)
